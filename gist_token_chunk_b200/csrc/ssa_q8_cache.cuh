@@ -85,6 +85,18 @@ struct Vec8<float> {
     }
 };
 
+// The rows [lo, hi) of block blk that a span of `count` rows from `start` holds;
+// false: none. In 64 bits until the block is known to hold some: a grid for T rows
+// has blocks past a shorter span's end, and near the largest N those start past 2^31.
+__host__ __device__ __forceinline__ bool rows_in_block(int start, int count, long long blk, int R,
+                                                       int& lo, int& hi) {
+    const long long b0 = blk * R, end = (long long)start + count;
+    if (b0 >= end || b0 + R <= start) return false;
+    lo = (int)(b0 > start ? b0 : start);
+    hi = (int)(b0 + R < end ? b0 + R : end);
+    return lo < hi;
+}
+
 __device__ __forceinline__ bool finite_bits(float x) {
     return (__float_as_uint(x) & 0x7fffffffu) < 0x7f800000u;
 }
@@ -147,11 +159,10 @@ __global__ void __launch_bounds__(GROUP == 32 ? 128 : GROUP) append_kernel(Appen
         if (tid == 0) atomicCAS(status, 0, (int)SSA_ERR_DEVICE_STATUS);
         return;
     }
-    const int blk = (int)a.by_rows.div(start) + blk_i;
-    const long long b0 = (long long)blk * a.R;              // first row of the block
-    const int lo = (int)max(b0, (long long)start);          // its new rows [lo, hi)
-    const int hi = (int)min(b0 + a.R, (long long)start + count);
-    if (lo >= hi) return;
+    const long long blk = (long long)a.by_rows.div(start) + blk_i;
+    const long long b0 = blk * a.R;  // first row of the block
+    int lo, hi;                      // its new rows
+    if (!rows_in_block(start, count, blk, a.R, lo, hi)) return;
     const int nv = (hi - lo) * VR;
     const long long rs = a.xs[kv][2];
     // vector tid of the new rows, and its place; vector tid + i GROUP is i steps on

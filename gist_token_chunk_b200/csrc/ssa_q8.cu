@@ -26,8 +26,7 @@ void clear_error() { g_err[0] = 0; }
 
 // First error since the last read; the kernels get it as an argument.
 static __device__ int g_status = 0;
-static __device__ int g_status_taken = 0;
-static __global__ void take_status_kernel() { g_status_taken = atomicExch(&g_status, 0); }
+static __global__ void take_status_kernel(int* taken) { *taken = atomicExch(&g_status, 0); }
 
 // Device address of g_status on the current device, looked up once per device.
 static cudaError_t status_ptr(int** p) {
@@ -429,12 +428,16 @@ SSA_API ssa_status ssa_decode_q8(const ssa_shape* shape, const void* q, const ui
 SSA_API ssa_status ssa_cache_get_status(int32_t* host_code, cudaStream_t stream) {
     clear_error();
     if (!host_code) return fail(SSA_ERR_INVALID_ARG, "ssa_cache_get_status: NULL output");
-    take_status_kernel<<<1, 1, 0, stream>>>();
-    cudaError_t e = cudaGetLastError();
-    int v = 0;
-    if (e == cudaSuccess)
-        e = cudaMemcpyFromSymbolAsync(&v, g_status_taken, sizeof(int), 0, cudaMemcpyDeviceToHost,
-                                      stream);
+    // a word of the call's own: readers on several streams never see each other's
+    int v = 0, *taken = nullptr;
+    cudaError_t e = cudaMallocAsync(reinterpret_cast<void**>(&taken), sizeof(int), stream);
+    if (e == cudaSuccess) {
+        take_status_kernel<<<1, 1, 0, stream>>>(taken);
+        e = cudaGetLastError();
+        if (e == cudaSuccess)
+            e = cudaMemcpyAsync(&v, taken, sizeof(int), cudaMemcpyDeviceToHost, stream);
+        cudaFreeAsync(taken, stream);
+    }
     if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess)
         return fail(SSA_ERR_CUDA, "ssa_cache_get_status: %s", cudaGetErrorString(e));

@@ -581,8 +581,24 @@ def ssa_decode_q8(q, k_raw, v_raw, k_gist, v_gist, k_raw_scale, v_raw_scale, k_g
                                  ws, *_on(stream)), "ssa_decode_q8")
 
 
-def ssa_cache_get_status(stream=None) -> int:
+def ssa_cache_get_status(stream=None, device=None) -> int:
+    """The status word of one device, read and cleared: the device of a torch stream, else
+    `device` (an index, name or torch.device), else the current one.  The calls record errors on
+    their tensors' device."""
+    if isinstance(stream, torch.cuda.Stream):
+        if device is not None and torch.device("cuda", stream.device_index) != _cuda_device(device):
+            raise ValueError(f"the stream is on cuda:{stream.device_index}, not on {device}")
+        device = stream.device_index
     code = _I(0)
-    _check_q8(lib.ssa_cache_get_status(ctypes.byref(code), _stream(stream)),
-              "ssa_cache_get_status")
+    with torch.cuda.device(None if device is None else _cuda_device(device)):
+        _check_q8(lib.ssa_cache_get_status(ctypes.byref(code), _stream(stream)),
+                  "ssa_cache_get_status")
     return int(code.value)
+
+
+def _cuda_device(device) -> torch.device:
+    """An index, name or torch.device as a device with its index."""
+    d = torch.device("cuda", device) if isinstance(device, int) else torch.device(device)
+    if d.type != "cuda":
+        raise ValueError(f"{device} is not a CUDA device")
+    return d if d.index is not None else torch.device("cuda", torch.cuda.current_device())

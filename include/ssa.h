@@ -651,10 +651,11 @@ SSA_API ssa_status ssa_workspace_size_q8(const ssa_shape* shape, int32_t C, int3
                                          int32_t topk, size_t* bytes);
 
 /*
- * Synchronise `stream`, return in *host_code the 8-bit cache calls' device
- * status word (SSA_OK or SSA_ERR_DEVICE_STATUS: the first error since the last
- * read) and clear it.  These calls keep their own word; ssa_get_device_status
- * does not see it.
+ * Synchronise `stream`, return in *host_code the 8-bit cache calls' status word
+ * of the current device (SSA_OK or SSA_ERR_DEVICE_STATUS: the first error since
+ * the last read) and clear it.  Of several threads that read at once, one gets
+ * the error.  These calls keep their own word; ssa_get_device_status does not
+ * see it.
  */
 SSA_API ssa_status ssa_cache_get_status(int32_t* host_code, cudaStream_t stream);
 

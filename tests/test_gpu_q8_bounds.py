@@ -52,3 +52,36 @@ def test_append_at_the_end_of_the_largest_cache(ssa):
     assert not bool(k[:, :, n:].any())
     del code, scale
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------- status word ---
+
+def test_two_readers_of_the_status_word(ssa):
+    """Two threads read on streams of their own: an error reaches exactly one of them."""
+    import threading
+
+    x = torch.ones(1, 1, 1, 64, device="cuda", dtype=torch.bfloat16)
+    c = torch.zeros(1, 1, 8, 64, dtype=torch.uint8, device="cuda")
+    s = torch.ones(1, 1, 1, device="cuda")
+    bad, rounds = i32([9]), 400
+    got = [[], []]
+    gate = threading.Barrier(2)
+
+    def read(i):
+        stream = torch.cuda.Stream()
+        for _ in range(rounds):
+            if i == 0:
+                ssa.ssa_cache_append_q8(x, None, bad, c, None, s, None)
+                torch.cuda.synchronize()
+            gate.wait(60)
+            got[i].append(ssa.ssa_cache_get_status(stream))
+            gate.wait(60)
+
+    threads = [threading.Thread(target=read, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(got[0]) == len(got[1]) == rounds
+    err = ssa.SSA_ERR_DEVICE_STATUS
+    assert all(sorted(p) == [0, err] for p in zip(*got))

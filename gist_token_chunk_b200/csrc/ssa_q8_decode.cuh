@@ -63,8 +63,8 @@ constexpr int kGistWeight = 5, kRawWeight = 8;
 constexpr int kStages = 3;
 template <int D>
 constexpr int kGroup = 128 / D;    // tiles of a stage
-// A partial result of one head: o[D], then the references of the weights and
-// of the sum, and the sum.  In shared memory the D / 8 columns that a lane holds
+// A partial result of one head: o[D], held over 2^(y + x), then y, x, and the sum, held
+// over 2^x.  y stays apart: past 2^24 a logit's 32 bits do not hold x + y.  In shared memory the D / 8 columns that a lane holds
 // lie 4 words further apart, and so do the records: stores of 16 bytes then share no
 // bank.
 template <int D>
@@ -1004,8 +1004,8 @@ __global__ void __launch_bounds__(32 * kWarps, kResident<D>) attend_kernel(Decod
             *reinterpret_cast<float4*>(mine + (2 * t + e) * CS + i) =
                 make_float4(acc[i][e] + acc[i][2 + e], acc[i + 1][e] + acc[i + 1][2 + e],
                             acc[i + 2][e] + acc[i + 2][2 + e], acc[i + 3][e] + acc[i + 3][2 + e]);
-    if (t == 0)  // log2 of what o is held over, without kWeightUp
-        *reinterpret_cast<float4*>(mine + 8 * CS) = make_float4(m + (float)top, m, l, 0.0f);
+    if (t == 0)
+        *reinterpret_cast<float4*>(mine + 8 * CS) = make_float4((float)top, m, l, 0.0f);
     __syncthreads();
     float* part = a.part + (long long)blockIdx.x * kHeads * W;
     for (int i = 4 * tid; i < heads * D; i += 4 * 32 * kWarps) {
@@ -1015,10 +1015,15 @@ __global__ void __launch_bounds__(32 * kWarps, kResident<D>) attend_kernel(Decod
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             r[w] = *reinterpret_cast<const float4*>(merge + (w * kHeads + h) * J + 8 * CS);
-            ty = fmaxf(ty, r[w].x);
             tx = fmaxf(tx, r[w].y);
         }
-        const float ry = ty == -INFINITY ? 0.0f : ty, rx = tx == -INFINITY ? 0.0f : tx;
+        const float rx = tx == -INFINITY ? 0.0f : tx;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            r[w].x += r[w].y - rx;
+            ty = fmaxf(ty, r[w].x);
+        }
+        const float ry = ty == -INFINITY ? 0.0f : ty;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         float sum = 0.0f;
 #pragma unroll
@@ -1033,7 +1038,7 @@ __global__ void __launch_bounds__(32 * kWarps, kResident<D>) attend_kernel(Decod
             sum += ex2(r[w].y - rx) * r[w].z;
         }
         if (ns == 1) {
-            const float f = exp2f(ry - rx) * (1.0f / kWeightUp) / sum;
+            const float f = exp2f(ry) * (1.0f / kWeightUp) / sum;
             out[i] = o.x * f;
             out[i + 1] = o.y * f;
             out[i + 2] = o.z * f;
@@ -1082,26 +1087,28 @@ __global__ void __launch_bounds__(32 * kWarps, kResident<D>) attend_kernel(Decod
                 }
         };
         fetch_some(0);
-        float ty = -INFINITY, tx = -INFINITY, sum = 0.0f;
+        auto refs = [&](int s) {
+            return __ldcg(reinterpret_cast<const float4*>(rec + (long long)s * kHeads * W + D));
+        };
+        const float4 f0 = refs(min(lane, ns - 1));  // most units have no more splits than that
+        float ty = -INFINITY, tx = f0.y, sum = 0.0f;
+        for (int s = lane + 32; s < ns; s += 32) tx = fmaxf(tx, refs(s).y);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) tx = fmaxf(tx, __shfl_xor_sync(0xffffffffu, tx, o));
+        const float rx = tx == -INFINITY ? 0.0f : tx;
         for (int s = lane; s < ns; s += 32) {
-            const float4 f = __ldcg(reinterpret_cast<const float4*>(rec + (long long)s * kHeads * W + D));
-            weight[s] = f.x;
-            ty = fmaxf(ty, f.x);
-            // the sum over its own running reference
-            const float nx = fmaxf(tx, f.y), ref = nx == -INFINITY ? 0.0f : nx;
-            sum = sum * ex2(tx - ref) + f.z * ex2(f.y - ref);
-            tx = nx;
+            const float4 f = s == lane ? f0 : refs(s);
+            const float y = f.x + (f.y - rx);
+            weight[s] = y;
+            ty = fmaxf(ty, y);
+            sum += f.z * ex2(f.y - rx);
         }
-        const float mine = tx;
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
             ty = fmaxf(ty, __shfl_xor_sync(0xffffffffu, ty, o));
-            tx = fmaxf(tx, __shfl_xor_sync(0xffffffffu, tx, o));
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
         }
-        const float ry = ty == -INFINITY ? 0.0f : ty, rx = tx == -INFINITY ? 0.0f : tx;
-        sum *= ex2(mine - rx);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float ry = ty == -INFINITY ? 0.0f : ty;
         __syncwarp();
         float o[V];
 #pragma unroll
@@ -1116,7 +1123,7 @@ __global__ void __launch_bounds__(32 * kWarps, kResident<D>) attend_kernel(Decod
                 }
             if (s0 + N < ns) fetch_some(s0 + N);
         }
-        const float up = exp2f(ry - rx) * (1.0f / kWeightUp);
+        const float up = exp2f(ry) * (1.0f / kWeightUp);
 #pragma unroll
         for (int i = 0; i < V; ++i) out[h * D + V * lane + i] = o[i] / sum * up;
         __syncwarp();

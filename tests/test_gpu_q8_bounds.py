@@ -1,5 +1,7 @@
 """The 8-bit cache and the rotation at the ends of their ranges, on the GPU, against
 64-bit references."""
+import functools
+
 import numpy as np
 import pytest
 import torch
@@ -85,3 +87,120 @@ def test_two_readers_of_the_status_word(ssa):
     assert len(got[0]) == len(got[1]) == rounds
     err = ssa.SSA_ERR_DEVICE_STATUS
     assert all(sorted(p) == [0, err] for p in zip(*got))
+
+
+# ------------------------------------------------------------------ decode ---
+#
+# What the decode may be off by, for each output on its own (u = 2^-24): a logit is off by
+# e = (d/8 + 8) u A, A = max over rows of sum |q_i k_i| / sqrt(d). The same weights are summed
+# and averaged, so that moves an output by e sum w |v - out|; the exponential and the weights'
+# 22 bits, the additions (rows / 64 + 8 of 2 u) add a share of sum w |v|. A weight times its
+# value scale is held to 2^-32 of the largest such product, and a weight under 2^-126 of the
+# largest may be taken as zero.
+
+def spread_reference(x, case, b, j, sel):
+    """Outputs of one (sequence, KV head) for a selection, and the bound of each."""
+    B, Hq, Hkv, d, n_max, C, g, topk, lens, dtype = case
+    G, n = Hq // Hkv, lens[b]
+    M = n // C
+    q = x["q"][b, j * G:(j + 1) * G].double().numpy()
+    mine = np.asarray([m for m in sel if m >= 0], np.int64)
+    keep = np.ones(M, bool)
+    keep[mine] = False
+    raw = np.concatenate([np.arange(m * C, m * C + C) for m in mine] + [np.arange(M * C, n)]).astype(np.int64)
+    gist = np.repeat(keep, g).nonzero()[0]
+
+    def rows(name):
+        code = np.concatenate([q8_ref.TABLE[x[f"{name}_gist"][b, j][gist]], q8_ref.TABLE[x[f"{name}_raw"][b, j][raw]]])
+        s = np.concatenate([x[f"{name}_gist_scale"][b, j][gist // g], x[f"{name}_raw_scale"][b, j][raw // C]])
+        return code, s.astype(np.float64)[:, None]
+
+    (kc, ks), (vc, vs) = rows("k"), rows("v")
+    lx = q @ (kc * ks).T / np.sqrt(d)
+    w = np.exp(lx - lx.max(1, keepdims=True))
+    w /= w.sum(1, keepdims=True)
+    v = vc * vs
+    out = w @ v
+    e = (d / 8 + 8) * U * (np.abs(q) @ np.abs(kc * ks).T).max(1, keepdims=True) / np.sqrt(d)
+    off = np.stack([(w[h][:, None] * np.abs(v - out[h])).sum(0) for h in range(G)])
+    tol = e * off * 1.01 + (w @ np.abs(v)) * (2.0 ** -20 + (len(v) / 64 + 8) * 2 * U)
+    floor = 2.0 ** -32 * (w * vs.T).max(1, keepdims=True) + 2.0 ** -125 * vs.T
+    return out, tol + floor @ np.abs(vc)
+
+
+U = 2.0 ** -24
+
+
+def check_spread(ssa, x, case):
+    from test_gpu_q8 import gpu_args
+
+    B, Hq, Hkv, d, n_max, C, g, topk, lens, dtype = case
+    G = Hq // Hkv
+    out, sel = ssa.ssa_decode_q8(*gpu_args(x, case))
+    assert ssa.ssa_cache_get_status() == 0
+    out, sel = out.cpu().double().numpy(), sel.cpu().numpy()
+    for b in range(B):
+        for j in range(Hkv):
+            ref, tol = spread_reference(x, case, b, j, sel[b, j])
+            err = np.abs(out[b, j * G:(j + 1) * G] - ref)
+            assert (err <= tol).all(), (b, j, (err / np.maximum(tol, 1e-300)).max(), err.max())
+
+
+SPREAD = [
+    (1, 4, 1, 64, 1024, 64, 8, 4, (1000,), "bf16"),
+    (1, 8, 1, 128, 1024, 64, 8, 4, (1000,), "fp32"),
+    (2, 4, 2, 64, 16384, 64, 8, 16, (16300, 5000), "bf16"),   # many splits
+    (1, 12, 1, 128, 8192, 128, 8, 8, (8100,), "bf16"),        # two head groups
+]
+
+
+@functools.lru_cache(maxsize=None)
+def made_once(case):
+    from test_gpu_q8 import decode_inputs
+
+    return decode_inputs(case, seed=30)
+
+
+def inputs(case):
+    return {k: v.copy() if isinstance(v, np.ndarray) else v for k, v in made_once(case).items()}
+
+
+def sharp_inputs(case, logit, place):
+    """Queries along one dim each, and for each head one row, at `place`, with that logit; all
+    others 0. Values at random."""
+    B, Hq, Hkv, d, n_max, C, g, topk, lens, dtype = case
+    G = Hq // Hkv
+    x = inputs(case)
+    x["q"] = torch.zeros(B, Hq, d)
+    for h in range(Hq):
+        x["q"][:, h, h % G] = logit * d ** 0.5 / 256
+    x["q"] = x["q"].to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    for n in ("k_raw", "k_gist"):
+        x[n][:] = 0
+        x[n + "_scale"][:] = 1.0
+    for b in range(B):
+        M = lens[b] // C
+        for h in range(G):
+            # the ties of the scores select the first chunks: chunk 1 is selected, M - 2 is not
+            if place == "raw":
+                x["k_raw"][b, :, C + 3 * h + 1, h] = 0x78  # 256
+            elif place == "gist":
+                x["k_gist"][b, :, (M - 2) * g + h % g, h] = 0x68  # 64: under the first chunks'
+                x["k_gist"][b, :, :topk * g, h] = 0x68
+            else:
+                x["k_raw"][b, :, lens[b] - 1 - h, h] = 0x78
+    return x
+
+
+@pytest.mark.parametrize("size", [1e6, 1e9, 1e12])
+@pytest.mark.parametrize("case", SPREAD)
+def test_decode_logits_past_24_bits(ssa, case, size):
+    """A logit so large that fp32 does not hold its sum with a scale's exponent: the output is the
+    row's value, whatever its scale."""
+    for place in ("raw", "tail"):
+        x = sharp_inputs(case, 256.0, place)
+        for n in ("k_raw_scale", "k_gist_scale"):
+            x[n][:] = np.float32(size / 256.0)
+        for n in ("v_raw_scale", "v_gist_scale"):
+            x[n][:] = 2.0 ** -9
+        check_spread(ssa, x, case)

@@ -122,6 +122,11 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// 2^e for a whole e up to 127; 0 under -126 (and for -inf and NaN).
+__device__ __forceinline__ float pow2(float e) {
+    return __uint_as_float((uint32_t)((int)fmaxf(e, -127.0f) + 127) << 23);
+}
+
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "

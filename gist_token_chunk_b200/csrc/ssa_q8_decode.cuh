@@ -49,12 +49,13 @@ constexpr int kSelectKeys = 16;    // keys of a thread that bisects
 constexpr int kMaxTopk = 1024;
 constexpr int kMaxSplits = 1024;   // splits of one (sequence, KV head, head group)
 constexpr int kMinTiles = 8;       // raw tiles of a split, as long as there are splits enough
-// Weights enter f16 over 2^(m + top): m may lag the true maximum by kLag (in
-// log2), so that few steps rescale the accumulators; top is the largest exponent of
-// the values' scales.  Times kWeightUp they stay under 2^(kLag + 1) kWeightUp = 2^15,
-// and f16's least step, 2^-24, is 2^-32 of the largest scale's weight.
-constexpr float kLag = 6.0f;
-constexpr float kWeightUp = 256.0f;
+// A softmax weight times its value scale enters f16 over a power of two that its head
+// raises when such a product passes kWeightMax: the largest is then put at 2^7 to 2^9, and
+// the next raise is a factor of 2^6 away.  So f16's least step, 2^-24, is under 2^-31 of
+// the largest product so far, half of it the most that a weight loses, whatever other
+// blocks' scales are (scales under 2^-100 count as that).
+constexpr float kWeightUp = 8.0f;  // log2
+constexpr float kWeightMax = 32768.0f, kSumMax = 1152921504606846976.0f;  // 2^15, 2^60
 // What a tile counts for in a split's share.  4, 5, 6, 8 to 8: 26.9, 26.1, 26.4, 27.8 us
 // (128K batch), 100.1, 84.5, 85.5, 86.8 (32 sequences).
 constexpr int kGistWeight = 5, kRawWeight = 8;
@@ -627,7 +628,7 @@ constexpr int kResident = D == 64 ? 4 : 3;
 template <class E, int D>
 __global__ void __launch_bounds__(32 * kWarps, kResident<D>) attend_kernel(DecodeArgs a, int* status) {
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ int plan[4 + kWarps];
+    __shared__ int plan[4];
     __shared__ typename QueryFrag<E, D>::Shared query;
     uint32_t* mask = reinterpret_cast<uint32_t*>(smem + a.smem_mask);
     int* sel = reinterpret_cast<int*>(smem + a.smem_sel);
@@ -796,13 +797,6 @@ __global__ void __launch_bounds__(32 * kWarps, kResident<D>) attend_kernel(Decod
             fetch(ring[i], first + i * P * kWarps);
             ++ahead;
         }
-    // value scales of its gists' chunks, of which the selection will drop some
-    uint32_t gs[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int at = g0 + tid + i * 32 * kWarps;
-        gs[i] = at < g1 ? __float_as_uint(__ldg(a.v_gist_s + pair * a.M_max + at)) & 0x7fffffffu : 0u;
-    }
     wait_prerequisites();
     __syncthreads();
     bool met = false;
@@ -822,31 +816,13 @@ __global__ void __launch_bounds__(32 * kWarps, kResident<D>) attend_kernel(Decod
         copies_end_group();
     }
 
-    // the largest value scale of this split's visible rows, while the copies fly
-    uint32_t big = 0u;
-    auto grow = [&](const float* sc, int i) { big = max(big, __float_as_uint(__ldg(sc + i)) & 0x7fffffffu); };
-    auto kept = [&](int i) { return !met || !((mask[(i - g0) >> 5] >> ((i - g0) & 31)) & 1u); };
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        if (gs[i] && kept(g0 + tid + i * 32 * kWarps)) big = max(big, gs[i]);
-    for (int i = g0 + tid + 2 * 32 * kWarps; i < g1; i += 32 * kWarps)
-        if (kept(i)) grow(a.v_gist_s + pair * a.M_max, i);
-    if (u1 > c.gist)
-        for (int i = (int)a.by_tpc.div(max(u0 - c.gist, 0)) + tid; i <= (int)a.by_tpc.div(u1 - 1 - c.gist);
-             i += 32 * kWarps)
-            grow(a.v_raw_s + pair * a.M_max, sel[i]);
-    big = __reduce_max_sync(0xffffffffu, big);
-    if (lane == 0) plan[4 + warp] = (int)big;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) big = max(big, (uint32_t)plan[4 + i]);
-    const int top = max(kMinScaleExp, min((int)(big >> 23) - 127, 126));
-    const float down = __uint_as_float((uint32_t)(127 - top) << 23) * kWeightUp;
-
-    const float qs = query.scale[gid];
-    // m: maximum of the logits (log2) so far, less kLag at most; l: sum of the weights
-    // p = 2^(x - m); a value's weight is p * scale.
-    float m = -INFINITY, l = 0.0f;
+    const bool here = gid < heads;
+    const float qs = here ? query.scale[gid] : 0.0f;
+    // The sum l of the weights p = 2^(x - m), and acc, the sum of p * scale * 2^(kWeightUp - k) *
+    // code. m and k are whole numbers. m is the maximum of the logits (log2) when it was last
+    // set; k is that of x - m + log2(scale), which m alone does not tell: the head may attend to
+    // blocks whose scales are far under others'.
+    float m = -INFINITY, k = -INFINITY, up = 0.0f, l = 0.0f;
     float acc[D / 8][4];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
@@ -861,7 +837,7 @@ __global__ void __launch_bounds__(32 * kWarps, kResident<D>) attend_kernel(Decod
         const Stage<D>& s = ring[slot];
         slot = slot == kStages - 1 ? 0 : slot + 1;
 
-        float x[P][4], vs[P][4], tx = -INFINITY;  // [tile][2 i + e]
+        float x[P][4], vs[P][4];  // [tile][2 i + e]
         uint32_t see[P];
 #pragma unroll
         for (int p = 0; p < P; ++p) {
@@ -890,10 +866,10 @@ __global__ void __launch_bounds__(32 * kWarps, kResident<D>) attend_kernel(Decod
             x[p][1] *= ks.y;
             x[p][2] *= ks.z;
             x[p][3] *= ks.w;
-            vs[p][0] = sv.x * down;
-            vs[p][1] = sv.y * down;
-            vs[p][2] = sv.z * down;
-            vs[p][3] = sv.w * down;
+            vs[p][0] = sv.x;
+            vs[p][1] = sv.y;
+            vs[p][2] = sv.z;
+            vs[p][3] = sv.w;
             // rows that exist and are not a selected chunk's gists
             const int rows = u + p < u1 ? s.rows[p] : 0;
             see[p] = rows >= kTile ? 0xffffu : (1u << rows) - 1u;
@@ -909,16 +885,46 @@ __global__ void __launch_bounds__(32 * kWarps, kResident<D>) attend_kernel(Decod
                         vs[p][i] = 0.0f;
                     }
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tx = fmaxf(tx, x[p][i]);
         }
-        tx = fmaxf(tx, __shfl_xor_sync(0xffffffffu, tx, 1));
-        tx = fmaxf(tx, __shfl_xor_sync(0xffffffffu, tx, 2));
-        if (__any_sync(0xffffffffu, tx > m + kLag)) {
-            const float nx = fmaxf(m, tx);
-            const float f = nx == -INFINITY ? 1.0f : ex2(m - nx);
-            m = nx;
-            l *= f;
+        float w[P][4], sum, most;
+        auto weigh = [&](float ref) {
+            sum = 0.0f;
+            most = 0.0f;
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float y = ex2(x[p][i] - ref);
+                    sum += y;
+                    w[p][i] = y * vs[p][i] * up;
+                    most = fmaxf(most, w[p][i]);
+                }
+        };
+        // with the references so far; the first tile finds none, and a NaN shows in the sum
+        weigh(m);
+        if (__any_sync(0xffffffffu, here && !(most <= kWeightMax && l + sum <= kSumMax))) {
+            float tx = -INFINITY, ty = -INFINITY;
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tx = fmaxf(tx, x[p][i]);
+            tx = fmaxf(tx, __shfl_xor_sync(0xffffffffu, tx, 1));
+            tx = fmaxf(tx, __shfl_xor_sync(0xffffffffu, tx, 2));
+            const float nx = fmaxf(m, ceilf(tx)), ref = nx == -INFINITY ? 0.0f : nx;
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int e = (int)(__float_as_uint(vs[p][i]) >> 23 & 255u) - 127;
+                    ty = fmaxf(ty, x[p][i] - ref + (float)max(e, kMinScaleExp));
+                }
+            ty = fmaxf(ty, __shfl_xor_sync(0xffffffffu, ty, 1));
+            ty = fmaxf(ty, __shfl_xor_sync(0xffffffffu, ty, 2));
+            // over the new m, acc's reference is `old`; what it holds is kept if that is the largest
+            const float old = m == -INFINITY ? -INFINITY : k + (m - nx);
+            const float nk = fmaxf(old, ceilf(ty));
+            const float f = nk == -INFINITY ? 0.0f : pow2(old - nk);
+            l *= pow2(m - nx);
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) {
                 acc[i][0] *= f;
@@ -926,23 +932,20 @@ __global__ void __launch_bounds__(32 * kWarps, kResident<D>) attend_kernel(Decod
                 acc[i][2] *= f;
                 acc[i][3] *= f;
             }
+            m = nx;
+            k = nk;
+            up = nk == -INFINITY ? 0.0f : pow2(kWeightUp - nk);
+            weigh(ref);
         }
-        const float ref = m == -INFINITY ? 0.0f : m;
+        l += sum;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             uint32_t hi[2], lo[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float w[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    w[e] = ex2(x[p][2 * i + e] - ref);
-                    l += w[e];
-                    w[e] *= vs[p][2 * i + e];
-                }
-                hi[i] = pack_f16(w[0], w[1]);
+                hi[i] = pack_f16(w[p][2 * i], w[p][2 * i + 1]);
                 const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi[i]));
-                lo[i] = pack_f16(w[0] - back.x, w[1] - back.y);
+                lo[i] = pack_f16(w[p][2 * i] - back.x, w[p][2 * i + 1] - back.y);
             }
             // the lane's D / 8 columns of rows t + 4 e + 8 i
             uint32_t v[2][2][D / 32];
@@ -1005,7 +1008,7 @@ __global__ void __launch_bounds__(32 * kWarps, kResident<D>) attend_kernel(Decod
                 make_float4(acc[i][e] + acc[i][2 + e], acc[i + 1][e] + acc[i + 1][2 + e],
                             acc[i + 2][e] + acc[i + 2][2 + e], acc[i + 3][e] + acc[i + 3][2 + e]);
     if (t == 0)
-        *reinterpret_cast<float4*>(mine + 8 * CS) = make_float4((float)top, m, l, 0.0f);
+        *reinterpret_cast<float4*>(mine + 8 * CS) = make_float4(k, m, l, 0.0f);
     __syncthreads();
     float* part = a.part + (long long)blockIdx.x * kHeads * W;
     for (int i = 4 * tid; i < heads * D; i += 4 * 32 * kWarps) {
@@ -1028,21 +1031,21 @@ __global__ void __launch_bounds__(32 * kWarps, kResident<D>) attend_kernel(Decod
         float sum = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float f = ex2(r[w].x - ry);
+            const float f = pow2(r[w].x - ry);
             const float4 y = *reinterpret_cast<const float4*>(merge + (w * kHeads + h) * J +
                                                               x / (D / 8) * CS + x % (D / 8));
             o.x += f * y.x;
             o.y += f * y.y;
             o.z += f * y.z;
             o.w += f * y.w;
-            sum += ex2(r[w].y - rx) * r[w].z;
+            sum += pow2(r[w].y - rx) * r[w].z;
         }
         if (ns == 1) {
-            const float f = exp2f(ry) * (1.0f / kWeightUp) / sum;
-            out[i] = o.x * f;
-            out[i + 1] = o.y * f;
-            out[i + 2] = o.z * f;
-            out[i + 3] = o.w * f;
+            const float r = 1.0f / sum, f = pow2(ry - kWeightUp);  // apart: both may be small
+            out[i] = o.x * r * f;
+            out[i + 1] = o.y * r * f;
+            out[i + 2] = o.z * r * f;
+            out[i + 3] = o.w * r * f;
         } else {
             __stcg(reinterpret_cast<float4*>(part + h * W + x), o);
             if (x == 0)
@@ -1101,7 +1104,7 @@ __global__ void __launch_bounds__(32 * kWarps, kResident<D>) attend_kernel(Decod
             const float y = f.x + (f.y - rx);
             weight[s] = y;
             ty = fmaxf(ty, y);
-            sum += f.z * ex2(f.y - rx);
+            sum += f.z * pow2(f.y - rx);
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) {
@@ -1117,15 +1120,15 @@ __global__ void __launch_bounds__(32 * kWarps, kResident<D>) attend_kernel(Decod
 #pragma unroll
             for (int s = 0; s < N; ++s)
                 if (s0 + s < ns) {
-                    const float f = ex2(weight[s0 + s] - ry);
+                    const float f = pow2(weight[s0 + s] - ry);
 #pragma unroll
                     for (int i = 0; i < V; ++i) o[i] += f * r[s][i];
                 }
             if (s0 + N < ns) fetch_some(s0 + N);
         }
-        const float up = exp2f(ry) * (1.0f / kWeightUp);
+        const float f = pow2(ry - kWeightUp);
 #pragma unroll
-        for (int i = 0; i < V; ++i) out[h * D + V * lane + i] = o[i] / sum * up;
+        for (int i = 0; i < V; ++i) out[h * D + V * lane + i] = o[i] / sum * f;
         __syncwarp();
     }
 }

@@ -192,6 +192,56 @@ def sharp_inputs(case, logit, place):
     return x
 
 
+@pytest.mark.parametrize("place", ["raw", "gist", "tail"])
+@pytest.mark.parametrize("case", SPREAD)
+def test_decode_weight_on_a_block_of_small_values(ssa, case, place):
+    """A head whose weight lies on one row of a block whose value scale is far under another
+    visible block's: the row's value to its own precision."""
+    B, Hq, Hkv, d, n_max, C, g, topk, lens, dtype = case
+    for logit, up in ((40, 12), (40, 20), (40, 30), (40, 40), (40, 60), (100, 100)):
+        x = sharp_inputs(case, logit * (4 if place == "gist" else 1), place)
+        for b in range(B):
+            M = lens[b] // C
+            for n in ("v_raw", "v_gist"):
+                x[n + "_scale"][b, :, :M + (n == "v_raw")] = 2.0 ** -20
+                x[n + "_scale"][b, :, M // 2] = 2.0 ** (up - 20)
+            x["v_raw_scale"][b, :, 2] = 2.0 ** (up - 20)
+        check_spread(ssa, x, case)
+
+
+@pytest.mark.parametrize("loud", [0.1, 1.0, 8.0])
+@pytest.mark.parametrize("case", SPREAD)
+def test_decode_value_scales_at_random(ssa, case, loud):
+    """Value scales over 80 powers of two, also of blocks beside each other."""
+    x = inputs(case)
+    x["q"] = x["q"] * loud
+    rnd = np.random.RandomState(int(loud * 10))
+    for n in ("v_raw_scale", "v_gist_scale"):
+        x[n] = np.where(np.isnan(x[n]), x[n], np.ldexp(1.0, rnd.randint(-40, 41, x[n].shape))).astype(np.float32)
+    check_spread(ssa, x, case)
+
+
+@pytest.mark.parametrize("step", [3.0, 30.0, -3.0])
+@pytest.mark.parametrize("case", SPREAD)
+def test_decode_logits_climb_while_values_shrink(ssa, case, step):
+    """Each chunk's logits `step` above the last one's and its values as much smaller, so that
+    all chunks count in the sums of the outputs and only the last in the softmax's."""
+    B, Hq, Hkv, d, n_max, C, g, topk, lens, dtype = case
+    x = inputs(case)
+    x["q"] = x["q"].clone()
+    M = n_max // C
+    x["q"][:] = 0
+    x["q"][:, :, 0] = d ** 0.5
+    for n in ("k_raw", "k_gist"):
+        x[n][:, :, :, 0] = 0x38  # 1
+        x[n][:, :, :, 1:] = 0
+        x[n + "_scale"][:] = (abs(step) * (np.arange(M) + 1 if step > 0 else M - np.arange(M))).astype(np.float32)
+    for n in ("v_raw_scale", "v_gist_scale"):
+        at = np.arange(M) if step > 0 else np.arange(M)[::-1]
+        x[n][:] = np.ldexp(1.0, np.clip(60 - np.round(abs(step) * at * 1.4427), -100, 60).astype(int)).astype(np.float32)
+    check_spread(ssa, x, case)
+
+
 @pytest.mark.parametrize("size", [1e6, 1e9, 1e12])
 @pytest.mark.parametrize("case", SPREAD)
 def test_decode_logits_past_24_bits(ssa, case, size):
@@ -203,4 +253,15 @@ def test_decode_logits_past_24_bits(ssa, case, size):
             x[n][:] = np.float32(size / 256.0)
         for n in ("v_raw_scale", "v_gist_scale"):
             x[n][:] = 2.0 ** -9
+        check_spread(ssa, x, case)
+
+
+@pytest.mark.parametrize("case", SPREAD)
+def test_decode_values_at_the_ends_of_fp32(ssa, case):
+    """Value scales of 2^-100, 2^100 and none that is a power of two, each alone and side by side."""
+    for scales in ((2.0 ** -100,), (2.0 ** 100,), (2.0 ** -100, 2.0 ** 100), (1.37e-12, 2.9e5, 0.71)):
+        x = inputs(case)
+        for n in ("v_raw_scale", "v_gist_scale"):
+            at = np.arange(x[n].shape[2])
+            x[n][:] = np.asarray(scales, np.float32)[at % len(scales)]
         check_spread(ssa, x, case)

@@ -166,7 +166,8 @@ struct QueryFrag {
                 w[0][i] = pack_f16(a, b);
                 if constexpr (NP == 2) {
                     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[0][i]));
-                    w[1][i] = pack_f16(a - f.x, b - f.y);
+                    // (an infinite element is all in the first part)
+                    w[1][i] = pack_f16(isinf(a) ? 0.0f : a - f.x, isinf(b) ? 0.0f : b - f.y);
                 }
             }
 #pragma unroll

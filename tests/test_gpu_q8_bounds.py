@@ -265,3 +265,33 @@ def test_decode_values_at_the_ends_of_fp32(ssa, case):
             at = np.arange(x[n].shape[2])
             x[n][:] = np.asarray(scales, np.float32)[at % len(scales)]
         check_spread(ssa, x, case)
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_decode_an_infinite_query_selects_by_its_sign(ssa, dtype, sign):
+    """One head's query has an infinite element: chunks with a gist key of its sign there score
+    +inf, the first of them are selected, and the other heads' outputs are as defined."""
+    from test_gpu_q8 import gpu_args
+
+    case = (1, 3, 1, 64, 2048, 32, 4, 6, (2000,), dtype)
+    x = inputs(case)
+    x["q"] = x["q"].clone()
+    x["q"][0, 1, 5] = sign * float("inf")
+    M, g = 2000 // 32, 4
+    rnd = np.random.RandomState(3)
+    code = np.where(rnd.rand(M, g) < 0.06, 0x30, 0xb0)  # 0.5, -0.5
+    code[7] = 0xb0
+    code[7, 2] = 0  # the product is NaN, which no maximum takes
+    x["k_gist"][0, 0, :M * g, 5] = code.ravel()
+    score = np.where(code == 0, -np.inf, sign * np.where(code == 0x30, np.inf, -np.inf)).max(1)
+    other = [x["q"][0, h].double().numpy() for h in (0, 2)]
+    keys = q8_ref.values(x["k_gist"][0, 0][None, None, :M * g], x["k_gist_scale"][0, 0][None, None, :M], g)[0, 0]
+    score = np.maximum(score, np.stack([keys @ q for q in other]).max(0).reshape(M, g).max(1))
+    want = np.sort(np.lexsort((np.arange(M), -score))[:6])
+    out, sel = ssa.ssa_decode_q8(*gpu_args(x, case))
+    assert np.array_equal(sel[0, 0].cpu().numpy(), want)
+    x["q"][0, 1] = 0.0
+    ref, tol = spread_reference(x, case, 0, 0, sel[0, 0].cpu().numpy())
+    out = out[0].cpu().double().numpy()
+    assert np.isnan(out[1]).all() and (np.abs(out - ref) <= tol)[[0, 2]].all()

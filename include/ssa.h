@@ -566,8 +566,8 @@ SSA_API ssa_status ssa_rope_freqs(int32_t rotary_dim, double base, int32_t scali
  *     w = p f_i,  (a, b) the dims of pair i in the layout,
  * and copies the other d - r (nothing to copy in place).  inverse != 0 takes -w:
  * the transposed map, which is also the gradient of the forward one.
- * Angles are taken in 64 bits, so every int32 position is exact to fp32; the
- * products are fp32, rounded once.
+ * Angles are reduced in twice 64 bits: at every position cosines and sines are
+ * within 2.6 * 2^-24 of those of p f_i.  The products are fp32, rounded once.
  * shape: B, Hq, Hkv, d, dtype of q and k (n_max is not used).  q holds T rows
  * of Hq heads a sequence, k (NULL: none) T rows of Hkv heads, with the strides
  * {sequence, head, row} in elements (HOST arrays of 3; the dims of a row are

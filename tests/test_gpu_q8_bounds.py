@@ -1,6 +1,8 @@
 """The 8-bit cache and the rotation at the ends of their ranges, on the GPU, against
 64-bit references."""
 import functools
+import math
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -295,3 +297,41 @@ def test_decode_an_infinite_query_selects_by_its_sign(ssa, dtype, sign):
     ref, tol = spread_reference(x, case, 0, 0, sel[0, 0].cpu().numpy())
     out = out[0].cpu().double().numpy()
     assert np.isnan(out[1]).all() and (np.abs(out - ref) <= tol)[[0, 2]].all()
+
+
+# ---------------------------------------------------------------- rotation ---
+
+def exact_turn(pos, freqs):
+    """Cosines and sines of pos * f, the product and its reduction exact, [rows, pairs]."""
+    two_pi = 2 * Fraction("3.14159265358979323846264338327950288419716939937510582097494459")
+    c, s = np.empty((len(pos), len(freqs))), np.empty((len(pos), len(freqs)))
+    for i, p in enumerate(pos):
+        for j, f in enumerate(freqs):
+            w = Fraction(int(p)) * Fraction(float(f))
+            w = float(w - round(w / two_pi) * two_pi)
+            c[i, j], s[i, j] = math.cos(w), math.sin(w)
+    return c, s
+
+
+@pytest.mark.parametrize("half", [True, False])
+def test_rope_angles_at_every_position(ssa, half):
+    """The rotation of unit pairs is the cosine and sine themselves, at near, far and the
+    farthest positions: the fraction in half turns is rounded to fp32 (2^-25, so pi / 2 u of
+    angle), sincospi is off by a step (u), the products are exact."""
+    rnd = np.random.RandomState(2)
+    pos = np.concatenate([np.arange(-3, 40), rnd.randint(0, 1 << 20, 60), rnd.randint(1 << 29, 2 ** 31 - 1, 60),
+                          2 ** 31 - 1 - np.arange(60), -2 ** 31 + np.arange(10)])
+    freqs, _ = ssa.ssa_rope_freqs(64, 10000.0)
+    c, s = exact_turn(pos, freqs.tolist())
+    i = np.arange(32)
+    a, b = (i, i + 32) if half else (2 * i, 2 * i + 1)
+    q = torch.zeros(1, 2, len(pos), 64)
+    q[:, 0, :, a] = 1.0
+    q[:, 1, :, b] = 1.0
+    layout = ssa.SSA_ROPE_HALF if half else ssa.SSA_ROPE_INTERLEAVED
+    for inverse in (False, True):
+        y, _ = ssa.ssa_rope(q.cuda(), None, i32(pos[None].tolist()), freqs.cuda(), layout, inverse=inverse)
+        y = y[0].cpu().double().numpy()
+        t = -s if inverse else s
+        for got, want in ((y[0][:, a], c), (y[0][:, b], t), (y[1][:, a], -t), (y[1][:, b], c)):
+            assert np.abs(got - want).max() <= 2.6 * U, np.abs(got - want).max() / U

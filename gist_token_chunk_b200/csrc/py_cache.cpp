@@ -128,6 +128,19 @@ struct Place {
     }
 };
 
+// Other Python threads run while this lives: an allocation may wait for the device, and
+// a launch for room in its queue. Made once the arguments are unpacked (the caller holds
+// the tensors); ended before a Python object is made, or by the exception that refuses.
+class NoGil {
+    PyThreadState* state_;
+
+public:
+    NoGil() : state_(PyEval_SaveThread()) {}
+    ~NoGil() { PyEval_RestoreThread(state_); }
+    NoGil(const NoGil&) = delete;
+};
+using Unlocked = std::optional<NoGil>;
+
 template <class T = void>
 T* want(const at::Tensor& t, const char* name, at::IntArrayRef shape, at::ScalarType type,
         const c10::Device& device) {
@@ -199,6 +212,7 @@ PyObject* rope(Args& a) {
     const at::Tensor* ko = a.maybe("k_out");
     PyObject* stream = a.next();
     Place at(q, stream, a.i32("stream_device"));
+    Unlocked gil(std::in_place);
     four_dims(q, "q");
     const int64_t B = q.size(0), Hq = q.size(1), T = q.size(2), d = q.size(3);
     if (k) four_dims(*k, "k");
@@ -229,6 +243,7 @@ PyObject* rope(Args& a) {
     const ssa_status st =
         api.rope(&shape, dim32(T), rq.p, rq.strides, rqo.p, rqo.strides, rk.p, rk.strides, rko.p, rko.strides,
                  p, rows, f, dim32(2 * freqs.numel()), layout, (float)scale, inverse, at.raw);
+    gil.reset();
     if (st != SSA_OK) return PyLong_FromLong(st);
     return pair(*qo, k ? ko : nullptr);
 }
@@ -273,6 +288,7 @@ PyObject* append(Args& a) {
     const at::Tensor* count = a.maybe("count");
     PyObject* stream = a.next();
     Place at(k, stream, a.i32("stream_device"));
+    Unlocked gil(std::in_place);
     four_dims(k, "k_new");
     const int64_t B = k.size(0), Hkv = k.size(1), T = k.size(2), d = k.size(3);
     const ssa_shape bare = {dim32(B), dim32(Hkv), dim32(Hkv), dim32(d), 0, dtype_code(k)};
@@ -288,6 +304,7 @@ PyObject* append(Args& a) {
     const int32_t* cp = count ? want<int32_t>(*count, "count", B, at::kInt, at.device) : nullptr;
     const ssa_status st = api.append(&shape, dim32(T), dim32(c.R), rk.p, rk.strides, rv.p, rv.strides, sp, cp,
                                      c.k, c.v, c.ks, c.vs, at.raw);
+    gil.reset();
     if (st != SSA_OK) return PyLong_FromLong(st);
     Py_RETURN_NONE;
 }
@@ -306,6 +323,7 @@ PyObject* read(Args& a) {
     const at::Tensor* vo = a.maybe("v_out");
     PyObject* stream = a.next();
     Place at(kc, stream, a.i32("stream_device"));
+    Unlocked gil(std::in_place);
     if (kc.dim() < 4) throw Refused("k_q8: wanted [B, Hkv, ..., d], got " + text(kc.sizes()));
     const int64_t B = kc.size(0), Hkv = kc.size(1), d = kc.size(-1);
     const Cache c(kc, vc, ks, vs, B, Hkv, d, at.device);
@@ -330,6 +348,7 @@ PyObject* read(Args& a) {
     const ssa_shape shape = {dim32(B), dim32(Hkv), dim32(Hkv), dim32(d), dim32(c.N), dtype_code(*ko)};
     const ssa_status st =
         api.read(&shape, T, dim32(c.R), c.k, c.v, c.ks, c.vs, sp, cp, kop, vop, at.raw);
+    gil.reset();
     if (st != SSA_OK) return PyLong_FromLong(st);
     return pair(*ko, vc ? vo : nullptr);
 }
@@ -353,13 +372,17 @@ PyObject* decode(Args& a) {
     const at::Tensor* ws = a.maybe("ws");
     PyObject* stream = a.next();
     Place at(q, stream, a.i32("stream_device"));
+    Unlocked gil(std::in_place);
     if (q.dim() != 3) throw Refused("q: wanted [B, Hq, d], got " + text(q.sizes()));
     four_dims(kr, "k_raw");
     const int64_t B = q.size(0), Hq = q.size(1), d = q.size(2), Hkv = kr.size(1), n_max = kr.size(2);
     const ssa_shape shape = {dim32(B), dim32(Hq), dim32(Hkv), dim32(d), dim32(n_max), dtype_code(q)};
     size_t need = 0;
     ssa_status st = api.workspace(&shape, C, g, topk, &need);  // checks the sizes
-    if (st != SSA_OK) return PyLong_FromLong(st);
+    if (st != SSA_OK) {
+        gil.reset();
+        return PyLong_FromLong(st);
+    }
     const int64_t M = n_max / C;
     const int64_t s_q[3] = {B, Hq, d}, s_raw[4] = {B, Hkv, n_max, d}, s_gist[5] = {B, Hkv, M, g, d};
     const int64_t s_scale[3] = {B, Hkv, M}, s_sel[3] = {B, Hkv, topk};
@@ -392,6 +415,7 @@ PyObject* decode(Args& a) {
     if (!ws->is_contiguous()) throw Refused("ws must be contiguous");
     st = api.decode(&shape, qp, krp, vrp, kgp, vgp, krsp, vrsp, kgsp, vgsp, lp, C, g, topk, op, selp,
                     ws->data_ptr(), ws->nbytes(), at.raw);
+    gil.reset();
     if (st != SSA_OK) return PyLong_FromLong(st);
     return pair(*out, sel);
 }

@@ -335,3 +335,43 @@ def test_rope_angles_at_every_position(ssa, half):
         t = -s if inverse else s
         for got, want in ((y[0][:, a], c), (y[0][:, b], t), (y[1][:, a], -t), (y[1][:, b], c)):
             assert np.abs(got - want).max() <= 2.6 * U, np.abs(got - want).max() / U
+
+
+# ------------------------------------------------------------ host threads ---
+
+def test_other_threads_run_while_a_launch_waits(ssa):
+    """Calls into a stream whose queue is full wait for room; the process's other threads do not."""
+    import threading
+    import time
+
+    x = torch.zeros(1, 1, 1, 64, device="cuda", dtype=torch.bfloat16)
+    c = torch.zeros(1, 1, 8, 64, dtype=torch.uint8, device="cuda")
+    s = torch.ones(1, 1, 1, device="cuda")
+    zero, stream = i32([0]), torch.cuda.Stream()
+    ssa.ssa_cache_append_q8(x, None, zero, c, None, s, None)
+    torch.cuda.synchronize()
+    gaps, stop = [], threading.Event()
+
+    def tick():
+        last = time.monotonic()
+        while not stop.is_set():
+            time.sleep(0.005)
+            now = time.monotonic()
+            gaps.append(now - last)
+            last = now
+
+    ticker = threading.Thread(target=tick)
+    ticker.start()
+    try:
+        with torch.cuda.stream(stream):
+            torch.cuda._sleep(3_000_000_000)  # about 1.5 s
+        t0 = time.monotonic()
+        for _ in range(3000):
+            ssa.ssa_cache_append_q8(x, None, zero, c, None, s, None, stream=stream)
+        waited = time.monotonic() - t0
+        torch.cuda.synchronize()
+    finally:
+        stop.set()
+        ticker.join()
+    assert waited > 0.8, "the queue was never full"
+    assert max(gaps) < 0.4, max(gaps)

@@ -2,7 +2,7 @@
 
 Compiles the CUDA kernels and the C ABI with nvcc into
 ``gist_token_chunk_b200/libssa.so`` (in-tree, static CUDA runtime), and the
-native part of the Python binding with g++ into ``gist_token_chunk_b200/_cache.so``.
+native part of the Python binding with g++ into ``binding_path()``.
 """
 from __future__ import annotations
 
@@ -20,8 +20,15 @@ HEADERS = ["ssa_device.cuh", "ssa_fused.cuh", "ssa_generic.cuh", "ssa_internal.h
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
-BINDING = os.path.join(HERE, "_cache.so")
 BINDING_SOURCE = os.path.join(CSRC, "py_cache.cpp")
+
+
+def binding_path() -> str:
+    """The binding for this Python and torch, whose binary interfaces it is tied to."""
+    import torch
+
+    tag = f"{sys.implementation.cache_tag}-torch-{torch.__version__}"
+    return os.path.join(HERE, f"_cache.{tag}.so")
 
 
 def _start_binding(force: bool):
@@ -31,16 +38,17 @@ def _start_binding(force: bool):
 
     import torch
 
+    path = binding_path()
     deps = [BINDING_SOURCE, os.path.join(ROOT, "include", "ssa.h"), os.path.abspath(__file__)]
-    if (not force and os.path.exists(BINDING)
-            and os.path.getmtime(BINDING) >= max(os.path.getmtime(d) for d in deps)):
+    if (not force and os.path.exists(path)
+            and os.path.getmtime(path) >= max(os.path.getmtime(d) for d in deps)):
         return None
     base = os.path.dirname(torch.__file__)
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     include = [os.path.join(base, "include"),
                os.path.join(base, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
-    tmp = BINDING + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-o", tmp,
            BINDING_SOURCE, f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
     cmd += [x for d in include for x in ("-isystem", d)]
@@ -76,7 +84,7 @@ def build(force: bool = False, verbose: bool = False, extra=(), out: str = LIB) 
     if binding is not None:
         if failed:
             raise subprocess.CalledProcessError(failed, binding[0].args)
-        os.replace(binding[1], BINDING)
+        os.replace(binding[1], binding_path())
     return out
 
 

@@ -17,10 +17,14 @@ budget ``ssa_adaptive_topk``, ``ssa_prefill_plan_size``, ``ssa_prefill_plan``,
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 from typing import Optional
 
 import torch
+
+from .build import binding_path
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # SSA_LIB_PATH selects another build of the same library (e.g. one compiled
@@ -32,11 +36,37 @@ if not os.path.exists(LIB_PATH):
         f"libssa.so not found at {LIB_PATH}: build it with gist_token_chunk_b200/build.py "
         "(or __graft_entry__.build()); there is no non-CUDA fallback")
 lib = ctypes.CDLL(LIB_PATH)
-try:
-    from . import _cache  # marshalling of the rotary and 8-bit cache calls (csrc/py_cache.cpp)
-except ImportError as e:
-    raise ImportError(f"gist_token_chunk_b200._cache cannot be loaded ({e}): build it with "
-                      "gist_token_chunk_b200/build.py (or __graft_entry__.build())") from e
+
+
+class _NoBinding:
+    """Stands for a binding that does not load: the calls that need it raise."""
+
+    def __init__(self, error):
+        self._error = error
+
+    def __getattr__(self, name):
+        raise ImportError(f"the binding of the rotary and 8-bit cache calls cannot be loaded "
+                          f"({self._error}): build it with gist_token_chunk_b200/build.py (or "
+                          "__graft_entry__.build())") from self._error
+
+
+def _load_binding():
+    """Marshalling of the rotary and 8-bit cache calls (csrc/py_cache.cpp)."""
+    try:
+        path = binding_path()
+        loader = importlib.machinery.ExtensionFileLoader(__package__ + "._cache", path)
+        spec = importlib.util.spec_from_file_location(loader.name, path, loader=loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+    except ImportError as e:
+        return _NoBinding(e)
+    module.bind(*[ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
+        "ssa_rope", "ssa_cache_append_q8", "ssa_cache_read_q8", "ssa_workspace_size_q8",
+        "ssa_decode_q8")])
+    return module
+
+
+_cache = _load_binding()
 
 SSA_OK = 0
 SSA_ERR_INVALID_ARG = 1
@@ -133,9 +163,6 @@ lib.ssa_cache_last_error.restype = ctypes.c_char_p
 for _f in ("ssa_rope_freqs", "ssa_rope", "ssa_cache_append_q8", "ssa_cache_read_q8",
            "ssa_workspace_size_q8", "ssa_decode_q8", "ssa_cache_get_status"):
     getattr(lib, _f).restype = _I
-_cache.bind(*[ctypes.cast(getattr(lib, _f), _P).value for _f in (
-    "ssa_rope", "ssa_cache_append_q8", "ssa_cache_read_q8", "ssa_workspace_size_q8",
-    "ssa_decode_q8")])
 for _f in ("ssa_adaptive_topk", "ssa_prefill_plan_size", "ssa_prefill_plan", "ssa_prefill",
            "ssa_prefill_get_status"):
     getattr(lib, _f).restype = _I

@@ -1,10 +1,13 @@
 """The Python side of the 8-bit cache calls without a GPU."""
 import contextlib
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
 
-from gist_token_chunk_b200 import ssa
+from gist_token_chunk_b200 import build, ssa
 
 
 class FakeCuda:
@@ -57,3 +60,37 @@ def test_status_takes_the_streams_device(monkeypatch):
     assert ssa.ssa_cache_get_status(s, device=1) == ssa.SSA_ERR_DEVICE_STATUS
     with pytest.raises(ValueError):
         ssa.ssa_cache_get_status(s, device=0)
+
+
+WITHOUT = """
+from gist_token_chunk_b200 import build
+build.binding_path = lambda: build.LIB + ".none"
+import torch
+from gist_token_chunk_b200 import ssa
+shape = ssa.make_shape(2, 8, 2, 64, 1024, ssa.SSA_BF16)
+assert ssa.ssa_workspace_size(shape, 64, 8, 4) > 0
+assert ssa.ssa_rope_freqs(64)[0].shape == (32,)
+try:
+    ssa.ssa_rope(torch.zeros(1, 1, 1, 64), None, torch.zeros(1), torch.zeros(32))
+except ImportError as e:
+    print("raised" if "build.py" in str(e) else e)
+"""
+
+
+def test_the_library_without_its_binding():
+    """A binding that does not load takes its own calls with it and no others."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", WITHOUT], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "raised", r.stderr[-2000:]
+
+
+def test_the_binding_is_built_for_its_torch(monkeypatch):
+    """Up to date for this Python and torch; another torch has it compiled anew."""
+    started = []
+    monkeypatch.setattr(build.subprocess, "Popen", lambda cmd: started.append(cmd))
+    assert build._start_binding(False) is None and not started
+    here = build.binding_path()
+    monkeypatch.setattr(torch, "__version__", "99.0")
+    assert build.binding_path() != here
+    _, out = build._start_binding(False)
+    assert started and out.startswith(build.binding_path())

@@ -217,7 +217,8 @@ SSA_API ssa_status ssa_rope_freqs(int32_t rotary_dim, double base, int32_t scali
         first = std::floor(pair_of(high));
         last = std::ceil(pair_of(low));
         if (first < 0.0) first = 0.0;
-        if (last > half - 1) last = half - 1;
+        // past the last pair, r/2 - 1, where that makes more than `low` turns itself
+        if (last > rotary_dim - 1) last = rotary_dim - 1;
         if (last <= first) last = first + 0.001;
     }
     for (int i = 0; i < half; ++i) {

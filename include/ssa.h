@@ -541,7 +541,8 @@ SSA_API const char* ssa_prefill_last_error(void);
                              turns between                                          */
 #define SSA_ROPE_RAMPED 3 /* f_i up to the pair that makes `high` turns over L,
                              f_i / factor from the pair that makes `low`, linear in i
-                             between (pairs rounded outwards, kept in [0, r/2 - 1]);
+                             between (pairs rounded outwards, kept in [0, r - 1]: the
+                             ramp may end past the last pair, r/2 - 1);
                              *scale = 0.1 ln(factor) + 1                            */
 /* Pair layouts of ssa_rope: pair i is (i, i + r/2), or (2 i, 2 i + 1). */
 #define SSA_ROPE_HALF 0

@@ -1,5 +1,6 @@
-"""The Python side of the 8-bit cache calls without a GPU."""
+"""The Python side of the rotary and 8-bit cache calls without a GPU."""
 import contextlib
+import math
 import os
 import subprocess
 import sys
@@ -94,3 +95,21 @@ def test_the_binding_is_built_for_its_torch(monkeypatch):
     assert build.binding_path() != here
     _, out = build._start_binding(False)
     assert started and out.startswith(build.binding_path())
+
+
+@pytest.mark.parametrize("length", [65536.0, 131072.0, 1e6, 1e9])
+def test_ramped_frequencies_of_a_long_original_length(length):
+    """A last pair that makes more than `low` turns is not slowed as if it made fewer: the ramp
+    ends past it, and no frequency falls when the original length grows."""
+    low, high, factor, r, base = 1.0, 32.0, 16.0, 64, 10000.0
+    f0, _ = ssa.ssa_rope_freqs(r, base)
+    f, _ = ssa.ssa_rope_freqs(r, base, ssa.SSA_ROPE_RAMPED, factor, low, high, length)
+    turns = length * f0 / (2 * math.pi)
+    first, last = (r * math.log(length / (2 * math.pi * n)) / (2 * math.log(base)) for n in (high, low))
+    first, last = max(math.floor(first), 0), min(math.ceil(last), r - 1)
+    assert float(turns[-1]) > low and last > r // 2 - 1
+    for i, (a, b) in enumerate(zip(f0.tolist(), f.tolist())):
+        w = min(max((i - first) / (last - first), 0.0), 1.0)
+        assert b == pytest.approx((1 - w) * a + w * a / factor, rel=1e-13)
+    shorter, _ = ssa.ssa_rope_freqs(r, base, ssa.SSA_ROPE_RAMPED, factor, low, high, length * 0.9)
+    assert (f >= shorter).all()

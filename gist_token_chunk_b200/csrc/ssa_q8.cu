@@ -141,8 +141,8 @@ static ssa_status plan_decode(DecodePlan& p, const ssa_shape* s, int32_t C, int3
     p.score_grid = pairs * ((M_max + a.nch - 1) / a.nch);
     // One CTA for each that is resident at a time, and up to four rounds of them
     // where each still has 64 tiles: then late CTAs even out what the rounding of
-    // splits per pair leaves.  32 sequences with d = 128: 84.5 us so (two rounds), 100.4
-    // with one, 93.1 from 32 tiles on; 512K batch 33.2, and 39.4 from 16 tiles on.
+    // splits per pair leaves.  32 sequences with d = 128: 82.6 us so (two rounds), 95.5
+    // with one, 91.0 from 32 tiles on; 512K batch 32.6, and 39.8 from 16 tiles on.
     const long long resident =
         (long long)ssa::sm_count() * (s->d == 64 ? kResident<64> : kResident<128>);
     const int k = topk < M_max ? topk : M_max;
@@ -207,8 +207,8 @@ static cudaError_t launch_decode(const DecodePlan& p, int* status, cudaStream_t 
     if (e != cudaSuccess) return e;
     if (a.topk > 0) {
         // One warp needs no barrier, and more take at least four: CTAs of two warps
-        // started and ran late next to the attention's (128K batch: 29.6 us a step
-        // with two, 26.1 with three or four; 32K batch 24.7 with one, 25.0 with four).
+        // started and ran late next to the attention's (128K batch: 29.2 us a step
+        // with two, 26.3 with four; 32K batch 24.2 with one, 24.8 with four).
         int warps = (a.M_max + 32 * kSelectKeys - 1) / (32 * kSelectKeys);
         warps = warps == 1 ? 1 : warps < 4 ? 4 : warps;
         const bool wide = 32 * warps > kSelThreads;

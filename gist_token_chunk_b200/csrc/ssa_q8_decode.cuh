@@ -1,5 +1,5 @@
-// ssa_q8_decode.cuh -- the decode step over the 8-bit cache, on the caller's
-// stream (every kernel but the first by programmatic dependent launch):
+// ssa_q8_decode.cuh -- the decode step over the 8-bit cache, three kernels on the
+// caller's stream by programmatic dependent launch:
 //
 //   score   x[m, t, h] = (q_h . code[m, t]) / sqrt(d) for every gist and head, kept,
 //           and s[m] = ks[m] * max over h and t, as an order-preserving key;
@@ -8,9 +8,10 @@
 //           logits and values), the selected chunks' raw rows and the tail, split
 //           over CTAs, joined by the last CTA of each (sequence, KV head).
 //
-// Bound by HBM: (M g + (M - k) g + 2 k C + 2 T) d bytes per (sequence, KV head).
-// Kept logits are 16 bytes a gist (G <= 4; else 32), written and read, in place of a
-// second read of its d bytes of key.
+// Bound by HBM: (M g + (M - k) g + 2 k C + 2 T) d bytes per (sequence, KV head). Heads go
+// in groups of eight, and above G = 8 everything but the gist keys is read once a group.
+// Kept logits are 16 bytes a gist (G <= 4; to 8 heads 32, above 64), written and read, in
+// place of a second read of its d bytes of key.
 // One block scale multiplies whole rows, so it never touches the codes: the
 // keys' scale multiplies the logit, the values' scale the softmax weight.
 // The codes become f16 (exact) in registers, on the way to m16n8k16.  Its
@@ -27,8 +28,8 @@
 // of the queries too, each time: the scores then issued 343 instructions for 16 rows.
 //
 // Measured (B200, us a step in a CUDA graph; in brackets the bytes at the copy's
-// rate): 32K batch 24.6 (6.4), 128K 26.1 (6.5), 512K 33.2 (10.2), 32 sequences with
-// d = 128 84.5 (41.6).  The first three are bound by the latencies of three dependent
+// rate): 32K batch 24.2 (6.4), 128K 26.3 (6.5), 512K 32.6 (10.2), 32 sequences with
+// d = 128 82.6 (41.6).  The first three are bound by the latencies of three dependent
 // kernels; the last by the attention's instructions a tile and its CTAs' start and end.
 #pragma once
 
@@ -41,8 +42,8 @@ constexpr int kHeads = 8;          // heads of one accumulator
 constexpr int kTile = 16;          // context rows a warp takes at a time
 constexpr int kWarps = 4;          // warps of an attend CTA
 constexpr int kScoreWarps = 4;
-// Gist rows of a score CTA (at least one chunk).  256, 512, 1024: 25.4, 24.6, 26.5 us a
-// step on the 32K batch, 26.1, 26.1, 27.9 on 128K, 86.0, 84.5, 86.0 on 32 sequences.
+// Gist rows of a score CTA (at least one chunk).  256, 512, 1024: 24.9, 24.2, 26.4 us a
+// step on the 32K batch, 26.3, 26.3, 28.1 on 128K, 84.4, 82.6, 84.4 on 32 sequences.
 constexpr int kScoreRows = 512;
 constexpr int kSelThreads = 512;
 constexpr int kSelectKeys = 16;    // keys of a thread that bisects
@@ -56,11 +57,11 @@ constexpr int kMinTiles = 8;       // raw tiles of a split, as long as there are
 // blocks' scales are (scales under 2^-100 count as that).
 constexpr float kWeightUp = 8.0f;  // log2
 constexpr float kWeightMax = 32768.0f, kSumMax = 1152921504606846976.0f;  // 2^15, 2^60
-// What a tile counts for in a split's share.  4, 5, 6, 8 to 8: 26.9, 26.1, 26.4, 27.8 us
-// (128K batch), 100.1, 84.5, 85.5, 86.8 (32 sequences).
+// What a tile counts for in a split's share.  4, 5, 6, 8 to 8: 27.0, 26.3, 26.4, 27.6 us
+// (128K batch), 95.7, 82.6, 83.7, 84.9 (32 sequences).
 constexpr int kGistWeight = 5, kRawWeight = 8;
-// A warp's ring: copies in flight, and the stage in use.  2, 3, 4: 32.9, 33.2, 44.0 us
-// (512K batch; four leave room for fewer CTAs), 87.9, 84.5, 84.8 (32 sequences).
+// A warp's ring: copies in flight, and the stage in use.  2, 3, 4: 32.1, 32.6, 43.1 us
+// (512K batch; four leave room for fewer CTAs), 87.3, 82.6, 81.9 (32 sequences).
 constexpr int kStages = 3;
 template <int D>
 constexpr int kGroup = 128 / D;    // tiles of a stage

@@ -304,7 +304,8 @@ SSA_API ssa_status ssa_rope(const ssa_shape* shape, int32_t T, const void* q,
     a.n = (long long)s.B * T * a.items;
     const long long blocks = (a.n + 255) / 256;
     if (blocks > INT32_MAX) return fail(SSA_ERR_UNSUPPORTED, "ssa_rope: too many rows");
-    // heads split over threads until the device is full (2048 threads an SM)
+    // heads split over threads until there are eight CTAs an SM; fewer are resident: two
+    // (bf16 half layout, 117 registers a thread), four (runs of 16 bytes otherwise) to six
     const long long want = (long long)ssa::sm_count() * 8;
     long long split = blocks >= want ? 1 : (want + blocks - 1) / blocks;
     if (split > a.H) split = a.H;

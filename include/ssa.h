@@ -529,8 +529,10 @@ SSA_API const char* ssa_prefill_last_error(void);
  * may hold anything: no call's result depends on them.
  *
  * The kernels are launched by programmatic dependent launch.  That leaves the
- * order of the stream as it is: each waits for the work before it in the stream
- * before it reads what that work may write, and before it writes.
+ * order of the stream as it is: a call's first kernel waits for the work before
+ * it before it reads or writes anything, and lets the call's next kernels start
+ * only then; those read the call's inputs at once, and wait for each other before
+ * they read what the call itself writes.
  */
 
 /* Frequency scalings of ssa_rope_freqs. */
@@ -630,9 +632,10 @@ SSA_API ssa_status ssa_cache_read_q8(const ssa_shape* shape, int32_t T, int32_t 
  * ssa_decode_q8 -- ssa_decode (same score, selection, context and outputs) on
  * the 8-bit cache.  shape->dtype is the queries' type; d in {64, 128}, Hq/Hkv
  * <= 16, topk <= 1024, g <= 1024, at most 2^19 chunks a sequence.  Logits,
- * softmax and sums are fp32; a softmax weight times its value scale enters the
- * product with the values in 22 bits, or to 2^-32 of its head's largest such
- * product where that is more (a scale under 2^-100 counts as that).  sel_idx may be NULL when topk = 0.
+ * softmax and sums are fp32.  A query element enters the product with the keys in
+ * 22 bits, or to 2^-38 of its head's largest element where that is more; a softmax
+ * weight times its value scale the product with the values in 22 bits, or to 2^-32
+ * of its head's largest such product (a scale under 2^-100 counts as that).  sel_idx may be NULL when topk = 0.
  * Needs ssa_workspace_size_q8() bytes of workspace, 256-byte aligned, which
  * needs no initialisation and may have served any other call (ws = NULL:
  * allocated stream-ordered).  Two calls that share a workspace must not run

@@ -635,7 +635,8 @@ SSA_API ssa_status ssa_cache_read_q8(const ssa_shape* shape, int32_t T, int32_t 
  * softmax and sums are fp32.  A query element enters the product with the keys in
  * 22 bits, or to 2^-38 of its head's largest element where that is more; a softmax
  * weight times its value scale the product with the values in 22 bits, or to 2^-32
- * of its head's largest such product (a scale under 2^-100 counts as that).  sel_idx may be NULL when topk = 0.
+ * of its head's largest such product (a scale under 2^-100 counts as that).  A
+ * softmax weight under 2^-126 of the largest may count as 0.  sel_idx may be NULL when topk = 0.
  * Needs ssa_workspace_size_q8() bytes of workspace, 256-byte aligned, which
  * needs no initialisation and may have served any other call (ws = NULL:
  * allocated stream-ordered).  Two calls that share a workspace must not run
